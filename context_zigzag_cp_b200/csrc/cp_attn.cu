@@ -1385,7 +1385,10 @@ extern "C" cp_status_t cp_attn_kv4(const cp_kv4_cache_t* c, int32_t num_heads, i
     P.T = n_queries;
     P.rows = static_cast<int32_t>(rows);
     P.causal = causal != 0;
-    P.window = window;
+    // no position is beyond the table (2^30 at most), so a wider window is this one, and the kernel's 32-bit
+    // position - window does not wrap
+    P.window = static_cast<int32_t>(
+        std::min<int64_t>(window, static_cast<int64_t>(c->table_width) * c->page_size + n_queries));
     P.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt(static_cast<float>(c->head_dim))) * 1.4426950408889634f;
     cudaStream_t s = as_stream(stream);
     // Row blocks of 4, 8 or 16 rows: the smallest that holds them all, else the largest whose O fits the registers.
