@@ -797,6 +797,8 @@ def attn_kv4(q, pages, block_table, seq_lens, causal=True, window=0, softmax_sca
         raise ValueError(f"q: shape {tuple(q.shape)}, the pages have {c.num_kv_heads} KV heads")
     if window < 0 or (window and not causal):
         raise ValueError(f"window: must not be negative, and needs causal=True; got {window}")
+    if window != int(window) or window > 0x7fffffff:
+        raise ValueError(f"window: a whole number up to 2^31 - 1 is needed, got {window}")
     _want(seq_lens, (B,), torch.int32, dev, "seq_lens")
     odt = torch.float32 if partial else torch.bfloat16
     if o is not None:
