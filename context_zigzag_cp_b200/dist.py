@@ -189,7 +189,15 @@ class ContextParallel:
 
         pages, block_table, seq_lens: this rank's part (cp_attn_kv4).  newest: the rank whose
         caches end with the T tokens themselves; the other ranks hold only tokens before
-        them, in any order (0 of them in a sequence is fine)."""
+        them, in any order (0 of them in a sequence is fine).
+
+        A problem with a window, with documents or without the causal mask is refused: the
+        parts' order does not say which of their keys such a mask leaves."""
+        for name, other in (("window", self.prob.window != 0), ("cu_seqlens", self.prob.cu_seqlens is not None),
+                            ("causal=False", not self.prob.causal)):
+            if other:
+                raise ValueError(f"decode: the problem has {name}; its caches' parts are attended whole, under the "
+                                 "causal mask")
         if not 0 <= newest < self.cp:
             raise ValueError(f"newest: {newest} is outside [0, {self.cp})")
         o, lse = self.kernels.attn_kv4(q, pages, block_table, seq_lens, self.rank == newest,
