@@ -5,7 +5,8 @@
 // For a row with partials (O_i, L_i):  m = max_i L_i,  w_i = exp(L_i - m)
 // (0 for L_i = -inf), L = m + ln sum_i w_i, O = sum_i w_i O_i / sum_i w_i.
 // This is the closed form of folding the partials pairwise in order; a row
-// whose partials are all -inf stays (0, -inf).
+// whose partials are all -inf stays (0, -inf), and one with a NaN among its L_i
+// is NaN (the maximum keeps it, where fmaxf would drop it).
 //
 // HBM-bound: each warp owns one row at a time; lane l reads columns
 // [4l, 4l+4) (and [128+4l, ...) for head_dim > 128) of each live partial with
@@ -18,6 +19,13 @@
 namespace cpattn {
 
 constexpr int MERGE_MAX_PARTS = 64;
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 struct MergeParams {
     int64_t rows;
@@ -39,8 +47,8 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(MergeParams M)
         // lane p holds L of parts p and p+32
         float la = lane < M.n_parts ? __ldg(M.lse_parts + static_cast<int64_t>(lane) * M.rows + row) : -INFINITY;
         float lb = lane + 32 < M.n_parts ? __ldg(M.lse_parts + static_cast<int64_t>(lane + 32) * M.rows + row) : -INFINITY;
-        float m = fmaxf(la, lb);
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        float m = max_nan(la, lb);
+        for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
         float4 acc0 = make_float4(0.f, 0.f, 0.f, 0.f), acc1 = acc0;
         float wsum = 0.f;
         if (m != -INFINITY) {
@@ -64,13 +72,13 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(MergeParams M)
                 }
             }
         }
-        const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+        const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
         uint2* dst = reinterpret_cast<uint2*>(M.o_out + row * M.D);
         if (lane < nvec)
             dst[lane] = make_uint2(pack_bf16(acc0.x * inv, acc0.y * inv), pack_bf16(acc0.z * inv, acc0.w * inv));
         if (two && lane + 32 < nvec)
             dst[lane + 32] = make_uint2(pack_bf16(acc1.x * inv, acc1.y * inv), pack_bf16(acc1.z * inv, acc1.w * inv));
-        if (lane == 0) M.lse_out[row] = wsum > 0.f ? m + logf(wsum) : -INFINITY;
+        if (lane == 0) M.lse_out[row] = wsum == 0.f ? -INFINITY : m + logf(wsum);
     }
 }
 
@@ -101,7 +109,7 @@ __global__ void __launch_bounds__(256) lse_merge_tiled_kernel(MergeParams M)
             for (int p = 0; p < M.n_parts; ++p) {
                 const float l = __ldg(M.lse_parts + static_cast<int64_t>(p) * M.rows + row);
                 w_s[p * 128 + r] = l;
-                m = fmaxf(m, l);
+                m = max_nan(m, l);
             }
             for (int p = 0; p < M.n_parts; ++p) {
                 const float l = w_s[p * 128 + r];
@@ -120,8 +128,8 @@ __global__ void __launch_bounds__(256) lse_merge_tiled_kernel(MergeParams M)
 #pragma unroll
                 for (int l = 0; l < off; ++l) v[l] = v[l] + v[l + off];
             const float wsum = m == -INFINITY ? 0.f : v[0];
-            inv_s[r] = wsum > 0.f ? 1.f / wsum : 0.f;
-            M.lse_out[row] = wsum > 0.f ? m + logf(wsum) : -INFINITY;
+            inv_s[r] = wsum == 0.f ? 0.f : 1.f / wsum;
+            M.lse_out[row] = wsum == 0.f ? -INFINITY : m + logf(wsum);
         }
         __syncthreads();
         const float inv = inv_s[r];

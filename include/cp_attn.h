@@ -267,7 +267,7 @@ CP_API cp_status_t cp_attn_bwd(const cp_problem_t* problem, const cp_plan_t* pla
  * (the concept guide's "combine(attn)", read as the exact log-sum-exp merge).
  *   o_parts    fp32 [n_parts][rows][head_dim]
  *   lse_parts  fp32 [n_parts][rows]; -inf marks a row with no key in that part
- *              (its O part is not read)
+ *              (its O part is not read), and a NaN makes the row NaN
  *   o_out      bf16 [rows][head_dim] (round to nearest even)
  *   lse_out    fp32 [rows]
  * head_dim must be a positive multiple of 4 no larger than 256; 1 <= n_parts
