@@ -1288,8 +1288,10 @@ extern "C" cp_status_t cp_rope(const cp_rope_t* r, const cp_problem_t* problem, 
         const int64_t n_out = cells * heads[i] * r->head_dim * 2;
         for (int k = 0; k < n_bufs; ++k) {
             const int64_t* st = in_strides + 3 * k;
-            const bool whole = st[2] == r->head_dim && st[1] == st[2] * r->rows &&
-                               (r->batch == 1 || st[0] == st[1] * heads[k]);
+            // contiguous; the stride of an extent of one says nothing (a caller may give 0)
+            const int64_t head = static_cast<int64_t>(r->rows) * r->head_dim;
+            const bool whole = (r->rows == 1 || st[2] == r->head_dim) && (heads[k] == 1 || st[1] == head) &&
+                               (r->batch == 1 || st[0] == head * heads[k]);
             if (k != i && overlap(out[k], cells * heads[k] * r->head_dim * 2, out[i], n_out)) return CP_ERR_INVALID_ARG;
             // a tensor may be rotated in place: each thread reads its own values before it writes them
             if (k == i && in[k] == out[i] && r->order == CP_ROPE_ROWS && whole) continue;

@@ -20,3 +20,26 @@ def test_windows_that_reach_beyond_every_key(lens, T, window):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     check_attn(q, pages, table, lens, *got, window=window)
     assert cz.get_device_status() == 0
+
+
+@pytest.mark.parametrize("B,H,N", [(1, 1, 1), (3, 1, 1), (3, 4, 1), (3, 1, 5), (1, 1, 5), (1, 4, 1), (1, 4, 5)])
+def test_in_place_where_an_extent_is_one(B, H, N):
+    """A contiguous tensor is rotated in place whatever its extents: a step's token, one KV head."""
+    D = 128
+    f = 10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64, device="cuda") / D)
+    pos = torch.arange(7, 7 + N, dtype=torch.int32, device="cuda")[None]
+    x, k = rows(B, H, N, D, 1).cuda(), rows(B, 2 * H, N, D, 2).cuda()
+    for kw in (dict(), dict(stream=torch.cuda.current_stream())):
+        want = cz.rope([x, k], f, positions=pos, **kw)
+        y, z = x.clone(), k.clone()
+        back = cz.rope([y, z], f, positions=pos, outs=[y, z], **kw)
+        assert back[0] is y and back[1] is z
+        assert torch.equal(y, want[0]) and torch.equal(z, want[1])
+    # not the same rows: an output that begins one token on, which a tensor of one row (D values) does not reach
+    flat = torch.zeros(B * H * N * D + D, dtype=torch.bfloat16, device="cuda")
+    call = lambda: cz.rope([flat[:-D].view(B, H, N, D)], f, positions=pos, outs=[flat[D:].view(B, H, N, D)])
+    if B * H * N == 1:
+        call()
+    else:
+        with pytest.raises(cz.CPError):
+            call()
