@@ -102,19 +102,19 @@ struct Kv4Token {
 template <int D>
 __device__ __forceinline__ bool kv4_token(const Kv4RowsParams& P, int b, int h, int t, Kv4Token& k)
 {
-    if (t >= P.T || (P.counts && t >= __ldg(P.counts + b))) return false;
-    k.row = P.rows ? __ldg(P.rows + t) : t;
+    if (t >= P.T || (P.counts && t >= P.counts[b])) return false;
+    k.row = P.rows ? P.rows[t] : t;
     if (k.row < 0 || k.row >= P.n_rows) {
         record_status(1 /* CP_ERR_INVALID_ARG */);
         return false;
     }
-    const int s = __ldg(P.start + b);
+    const int s = P.start[b];
     if (s < 0 || s > 0x7fffffff - t) {
         record_status(1 /* CP_ERR_INVALID_ARG */);
         return false;
     }
     const int pos = s + t, blk = pos >> 4, i = P.by_page.of(blk);
-    const int page = i < P.C.width ? __ldg(P.C.table + static_cast<int64_t>(b) * P.C.width + i) : -1;
+    const int page = i < P.C.width ? P.C.table[static_cast<int64_t>(b) * P.C.width + i] : -1;
     if (page < 0 || page >= P.C.num_pages) {
         record_status(1 /* CP_ERR_INVALID_ARG */);
         return false;

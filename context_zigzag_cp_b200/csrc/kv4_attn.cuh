@@ -128,7 +128,7 @@ __device__ __forceinline__ Kv4Span kv4_span_of(const Kv4AttnParams& P, int len)
 
 __device__ __forceinline__ Kv4Span kv4_span(const Kv4AttnParams& P, int b, bool report)
 {
-    const int len = __ldg(P.lens + b), room = P.C.width * P.C.page_size;   // at most 2^30
+    const int len = P.lens[b], room = P.C.width * P.C.page_size;   // at most 2^30
     const int cut = min(max(len, 0), room);
     if (report && cut != len) record_status(1 /* CP_ERR_INVALID_ARG */);
     return kv4_span_of(P, cut);
@@ -334,7 +334,7 @@ __device__ __forceinline__ void kv4_load_query(const Kv4AttnParams& P, int b, in
         const uint4* src =
             reinterpret_cast<const uint4*>(P.q + b * P.qs[0] + (h * (P.Hq / P.C.Hkv) + hg) * P.qs[1] + tok * P.qs[2]);
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) x[nt][w] = live ? __ldg(src + 4 * w + t) : make_uint4(0, 0, 0, 0);
+        for (int w = 0; w < D / 32; ++w) x[nt][w] = live ? src[4 * w + t] : make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -888,7 +888,7 @@ kv4_attn_kernel(Kv4AttnParams P)
             place = KV4_NONE;
             if (blk < blk1) {
                 const int i = P.by_page.of(blk);   // below the table's width: blk * 16 is below the length
-                const int page = __ldg(P.C.table + static_cast<int64_t>(b) * P.C.width + i);
+                const int page = P.C.table[static_cast<int64_t>(b) * P.C.width + i];
                 wrong = page < 0 || page >= P.C.num_pages;
                 if (wrong)
                     record_status(1 /* CP_ERR_INVALID_ARG */);
@@ -1131,7 +1131,7 @@ __global__ void __launch_bounds__(KV4_MERGE_WARPS<ROWS> * 32, ROWS == 16 ? 2 : 4
     __shared__ float2 sh_ml[W];
     // every CTA waits, also those with nothing to join: the grid must not be over before the first one
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 job = P.jobs[blockIdx.x];   // written by the kernel before: not __ldg
+    const int4 job = P.jobs[blockIdx.x];   // written by the kernel before
     const int parts = job.w;
     if (parts == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = warp / WPR, w0 = warp % WPR;

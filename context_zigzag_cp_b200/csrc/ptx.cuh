@@ -431,7 +431,9 @@ template <uint32_t N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // At the start of a kernel that is launched while the one before it ends: lets the next one do the same, then waits
-// until everything before is done and its writes can be seen.
+// until everything before is done and its writes can be seen.  Such a kernel is on the GPU while its inputs are still
+// written, so it reads them by plain loads after this: __ldg is for what nothing writes while the kernel lives, and the
+// compiler may move it ahead of the wait.
 __device__ __forceinline__ void grid_ahead()
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

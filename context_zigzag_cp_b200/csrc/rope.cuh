@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(256, HALF ? 2 : 4) rope_kernel(RopeParams P)
 
     int src = n;
     if (P.in_map) {
-        src = __ldg(P.in_map + n);
+        src = P.in_map[n];
         if (src < 0 || src >= P.in_rows) {
             record_status(1 /* CP_ERR_INVALID_ARG */);
             return;
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(256, HALF ? 2 : 4) rope_kernel(RopeParams P)
     }
     float cs[8], sn[8];
     if (turns) {
-        int orig = P.orig_map ? __ldg(P.orig_map + n) : n;
+        int orig = P.orig_map ? P.orig_map[n] : n;
         if (!P.positions) orig += P.row_base;
         int pos[ROPE_MAX_AXES];
         if (P.positions) {
@@ -109,9 +109,9 @@ __global__ void __launch_bounds__(256, HALF ? 2 : 4) rope_kernel(RopeParams P)
             }
 #pragma unroll
             for (int a = 0; a < ROPE_MAX_AXES; ++a)
-                pos[a] = a < P.n_axes ? __ldg(P.positions + b * P.pos_batch + a * P.pos_axis + orig) : 0;
+                pos[a] = a < P.n_axes ? P.positions[b * P.pos_batch + a * P.pos_axis + orig] : 0;
         } else {
-            if (P.doc_start) orig -= __ldg(P.doc_start + (P.shard_map ? __ldg(P.shard_map + n) : n));
+            if (P.doc_start) orig -= P.doc_start[P.shard_map ? P.shard_map[n] : n];
 #pragma unroll
             for (int a = 0; a < ROPE_MAX_AXES; ++a) pos[a] = orig;
         }
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256, HALF ? 2 : 4) rope_kernel(RopeParams P)
             for (int a = 1; a < ROPE_MAX_AXES; ++a)
                 if (a < P.n_axes && pair >= P.sec_end[a - 1]) p = pos[a];
             const unsigned long long t =
-                static_cast<unsigned long long>(static_cast<long long>(p)) * rope_turns(__ldg(P.inv_freq + pair));
+                static_cast<unsigned long long>(static_cast<long long>(p)) * rope_turns(P.inv_freq[pair]);
             float s, c;
             sincospif(static_cast<float>(static_cast<int>(t >> 32)) * 4.656612873077393e-10f, &s, &c);
             cs[i] = c;
