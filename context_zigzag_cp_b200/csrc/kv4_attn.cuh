@@ -38,8 +38,12 @@
 //     warps until all of a CTA's tiles are done.
 //   - m is a lazily moved reference: a stage raises it only when some score
 //     exceeds it by 8 (base 2), so the common stage needs one vote and no shuffles.
-//     p <= 2^8 then; P goes to fp16 as p scale 2^(6 - E), E the largest exponent of a
-//     V scale so far, hence at most 2^15, and 2^-39 of the largest still counts.
+//     p <= 2^8 then; P goes to fp16 as p scale 2^(6 - E), E the largest exponent of the V
+//     scales of the same 64 dims so far (a key without weight does not count), hence at most
+//     2^15: 11 bits down to 2^-20 of that scale, steps of 2^-30 of it below.  (One E for all
+//     dims gave 64 dims with values 2^30 below the others' an O of zeros.  An E for each 64
+//     costs nothing; leaving keys without weight out costs 0.1 of 5.2 us for 301 keys, 0.5 of
+//     119 us for 64 ragged sequences, 1 to 1.6 of 44 to 52 us at head_dim 256.)
 //   - One CTA of eight warps an SM and 64 keys computed together: two warps a scheduler fill
 //     the integer pipe as well as more do, and what a stage costs is paid half as often (64
 //     ragged sequences of up to 16k keys, 32 / 8 heads of 128 dims: 115 us = 5.9 TB/s; 16 warps and
@@ -319,13 +323,14 @@ struct Kv4Query {
     float mul[Cfg::NT][Cfg::NC];
 };
 
-// The lane's words of the rows of column g.
+// The lane's words of the rows of column g; of a row that is not there NaN, which counts in no maximum and no vote.
 template <int D, int ROWS>
 __device__ __forceinline__ void kv4_load_query(const Kv4AttnParams& P, int b, int h, int rb,
                                                uint4 (&x)[Kv4AttnCfg<D, ROWS>::NT][D / 32])
 {
     using Cfg = Kv4AttnCfg<D, ROWS>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint4 none = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
 #pragma unroll
     for (int nt = 0; nt < Cfg::NT; ++nt) {
         const int r = rb * ROWS + nt * 8 + (Cfg::PAIR ? g >> 1 : g);
@@ -334,7 +339,7 @@ __device__ __forceinline__ void kv4_load_query(const Kv4AttnParams& P, int b, in
         const uint4* src =
             reinterpret_cast<const uint4*>(P.q + b * P.qs[0] + (h * (P.Hq / P.C.Hkv) + hg) * P.qs[1] + tok * P.qs[2]);
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) x[nt][w] = live ? src[4 * w + t] : make_uint4(0, 0, 0, 0);
+        for (int w = 0; w < D / 32; ++w) x[nt][w] = live ? src[4 * w + t] : none;
     }
 }
 
@@ -403,7 +408,7 @@ __device__ __forceinline__ void kv4_make_query(const Kv4AttnParams& P, const uin
     }
 }
 
-// Running state of a warp.  O^T accumulators, m-tile by m-tile, in units of 2^-24 2^(e - 133):
+// Running state of a warp.  O^T accumulators, m-tile by m-tile, in units of 2^-24 2^(e - 133), e that of the group:
 //   PAIR: tile 2 gd + m, dims 64 gd + 8 g + (2m, 2m + 4; 2m + 1, 2m + 5) of row t;
 //   else: tile 4 gd + i, dims 64 gd + 8 g + 2i (and 2i + 1 in c + 2), columns 2t, 2t + 1;
 // the odd dims count 16 times.  Reference -m, and the lane's share of l, of the sum of p scale (as rounded
@@ -413,10 +418,12 @@ struct Kv4State {
     using Cfg = Kv4AttnCfg<D, ROWS>;
     float o[Cfg::NT][Cfg::OT][4];
     float nm[Cfg::NT][Cfg::NC], l[Cfg::NT][Cfg::NC], ps[Cfg::NT][D / 64][Cfg::NC], z[Cfg::NT][D / 64][Cfg::NC];
-    uint32_t e;   // biased exponent that the V scales in o are relative to
-    float down;   // 2^(6 - (e - 127))
-    float limit;  // 2^(e + 1 - 127), a scale that e is too small for (infinite: none)
+    float down[D / 64];   // 2^(133 - e), e the biased exponent that the V scales of a group are relative to in o and ps
 };
+
+// From 2^(133 - e): 2^(e - 133), and e.
+__device__ __forceinline__ float kv4_up(float down) { return __uint_as_float((254u << 23) - __float_as_uint(down)); }
+__device__ __forceinline__ int kv4_exp(float down) { return 260 - static_cast<int>(__float_as_uint(down) >> 23); }
 
 template <int D, int ROWS>
 __device__ __forceinline__ void kv4_clear(Kv4State<D, ROWS>& S)
@@ -436,9 +443,8 @@ __device__ __forceinline__ void kv4_clear(Kv4State<D, ROWS>& S)
             for (int i = 0; i < D / 64; ++i) S.ps[nt][i][c] = S.z[nt][i][c] = 0.f;
         }
     }
-    S.e = 27;
-    S.down = pow2i(106);
-    S.limit = pow2i(27 - 126);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) S.down[i] = pow2i(106);   // e = 27
 }
 
 // (scale, zero) pairs of one key.
@@ -530,6 +536,7 @@ __device__ __forceinline__ void kv4_step(const uint8_t* blk, const Kv4Query<D, R
     // ---- scores against the reference: x = s - m (base 2)
     float s[STEP][NT][2 * NC], x[STEP][NT][2 * NC];
     uint32_t vm[STEP][2][NG];   // V's (scale, zero) of keys g, g + 8
+    float vd[STEP][2][NG];      // V's scales times S.down
     float most = -INFINITY, top = 0.f;
 #pragma unroll
     for (int k = 0; k < STEP; ++k) {
@@ -559,19 +566,18 @@ __device__ __forceinline__ void kv4_step(const uint8_t* blk, const Kv4Query<D, R
 #pragma unroll
             for (int c = 0; c < 2 * NC; c += 2) most = fmax3(most, x[k][nt][c], x[k][nt][c + 1]);
 #pragma unroll
-        for (int i = 0; i < NG; ++i) top = fmax3(top, bf_lo(vm[k][0][i]), bf_lo(vm[k][1][i]));
+        for (int i = 0; i < NG; ++i) {
+            vd[k][0][i] = bf_lo(vm[k][0][i]) * S.down[i];
+            vd[k][1][i] = bf_lo(vm[k][1][i]) * S.down[i];
+            top = fmax3(top, vd[k][0][i], vd[k][1][i]);
+        }
     }
 
-    // ---- a new reference, or a larger exponent of V's scales (which are not negative)
-    if (__any_sync(0xffffffffu, most > 8.f || top >= S.limit)) {
-        const uint32_t et = min(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23, 254u);
-        const float fe = et > S.e ? pow2i(max(static_cast<int>(S.e) - static_cast<int>(et), -126)) : 1.f;
-        S.e = max(S.e, et);
-        S.down = pow2i(133 - static_cast<int>(S.e));
-        S.limit = pow2i(static_cast<int>(S.e) - 126);
+    // ---- a new reference, or other exponents of V's scales (which are not negative)
+    if (__any_sync(0xffffffffu, most > 8.f || top >= 128.f)) {
+        float f[NT][NC];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float fc[NC];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 float m = -S.nm[nt][c];
@@ -584,8 +590,7 @@ __device__ __forceinline__ void kv4_step(const uint8_t* blk, const Kv4Query<D, R
                             m = fmaxf(m, s[k][nt][c + NC * j] * Q.mul[nt][c]);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                const float f = old == -INFINITY ? 0.f : ex2(old - m);
-                fc[c] = f;
+                f[nt][c] = old == -INFINITY ? 0.f : ex2(old - m);
                 S.nm[nt][c] = -m;
 #pragma unroll
                 for (int k = 0; k < STEP; ++k)
@@ -593,18 +598,54 @@ __device__ __forceinline__ void kv4_step(const uint8_t* blk, const Kv4Query<D, R
                     for (int j = 0; j < 2; ++j)
                         if (!MASK || x[k][nt][c + NC * j] != -INFINITY)
                             x[k][nt][c + NC * j] = fmaf(s[k][nt][c + NC * j], Q.mul[nt][c], -m);
-                S.l[nt][c] *= f;
+                S.l[nt][c] *= f[nt][c];
+            }
+        // The exponent of a group's scales follows the largest, but not that of a key without weight, beside which the
+        // others would lose their bits: no further than 2^8 above the smallest of the lanes' largest scales or 2^10 above
+        // the largest p scale of the step.  It falls where it was 2^8 too large.  p <= 1 here, so p scale 2^(6 - E) < 2^7.
+        float p[STEP][2];   // largest weight of a key
 #pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    S.z[nt][i][c] *= f;
-                    S.ps[nt][i][c] *= f * fe;
-                }
+        for (int k = 0; k < STEP; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float y = x[k][0][NC * j];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) y = fmaxf(y, x[k][nt][NC * j + c]);
+                p[k][j] = ex2(y);
             }
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float f = fc[c & (NC - 1)] * fe;
+        for (int i = 0; i < NG; ++i) {
+            float v = 0.f, w = 0.f;
 #pragma unroll
-                for (int i = 0; i < Cfg::OT; ++i) S.o[nt][i][c] *= f;
+            for (int k = 0; k < STEP; ++k) {
+                v = fmax3(v, bf_lo(vm[k][0][i]), bf_lo(vm[k][1][i]));
+                w = fmax3(w, p[k][0] * bf_lo(vm[k][0][i]), p[k][1] * bf_lo(vm[k][1][i]));
+            }
+            const int most_e = min(__reduce_max_sync(0xffffffffu, __float_as_uint(v)) >> 23, 254u);
+            const int least_e = __reduce_min_sync(0xffffffffu, v > 0.f ? __float_as_uint(v) : 0x7f800000u) >> 23;
+            const int w_e = __reduce_max_sync(0xffffffffu, __float_as_uint(w)) >> 23;
+            const int old = kv4_exp(S.down[i]);
+            int e = min(most_e, max(max(w_e + 10, least_e + 8), old));   // most_e where it is no more than old
+            e = e >= old ? e : e > 0 && e + 7 < old ? max(e, max(old - 60, 27)) : old;
+            const float fe = pow2i(max(old - e, -126));
+            S.down[i] = pow2i(133 - e);
+#pragma unroll
+            for (int k = 0; k < STEP; ++k)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) vd[k][j][i] = bf_lo(vm[k][j][i]) * S.down[i];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    S.z[nt][i][c] *= f[nt][c];
+                    S.ps[nt][i][c] *= f[nt][c] * fe;
+                }
+#pragma unroll
+                for (int t = i * (Cfg::OT / NG); t < (i + 1) * (Cfg::OT / NG); ++t)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) S.o[nt][t][c] *= f[nt][c & (NC - 1)] * fe;
             }
         }
     }
@@ -629,7 +670,7 @@ __device__ __forceinline__ void kv4_step(const uint8_t* blk, const Kv4Query<D, R
         for (int i = 0; i < NG; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float sc = bf_lo(vm[k][j][i]), ze = fmaf(8.f, sc, bf_hi(vm[k][j][i])), sd = sc * S.down;
+                const float sc = bf_lo(vm[k][j][i]), ze = fmaf(8.f, sc, bf_hi(vm[k][j][i])), sd = vd[k][j][i];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float ps[NC];
@@ -749,13 +790,13 @@ __device__ __forceinline__ void kv4_rows_of(const Kv4State<D, ROWS>& S, F&& f)
 {
     using Cfg = Kv4AttnCfg<D, ROWS>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const float up = pow2i(static_cast<int>(S.e) - 133);
 #pragma unroll
     for (int nt = 0; nt < Cfg::NT; ++nt)
 #pragma unroll
         for (int c = 0; c < Cfg::NC; ++c)
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
+                const float up = kv4_up(S.down[i]);
                 float x[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {

@@ -551,8 +551,10 @@ CP_API cp_status_t cp_kv4_read(const cp_kv4_cache_t* cache, int32_t n_tokens, co
  * n_queries is 1..1024; the kernel is made for few (decoding, a handful of drafted
  * tokens): 16 rows (query heads of a KV head x tokens; 8 at head_dim 256) share a pass over the
  * keys.  The result does not depend on timing (fixed split, fixed order).
- * Query, weights and codes are multiplied in fp16 (a query value keeps its bits down to 2^-15 of the
- * largest of its 16 neighbours, weights are rounded to 11 bits); scores, the softmax's sums and O
+ * Query, weights and codes are multiplied in fp16: a query value keeps its bits down to 2^-15 of the
+ * largest of its 16 neighbours; a weight times its V scale is rounded to 11 bits down to 2^-20 of the
+ * largest V scale among the sequence's keys in the same 64 dims (keys that no row of the KV head
+ * gives weight do not count), and to 2^-31 of that scale below.  Scores, the softmax's sums and O
  * are held in 32 bits.  A query row with an infinity, a NaN or a value beyond 2^119 / scale gives NaN.
  * Workspace: partial results of sequences that several CTAs share (at most
  * 2 * CTAs * 16 rows of head_dim + 2 floats, and 16 bytes a CTA); none for a few short sequences.
