@@ -537,10 +537,12 @@ __device__ __forceinline__ void kv4_step(const uint8_t* blk, const Kv4Query<D, R
     float s[STEP][NT][2 * NC], x[STEP][NT][2 * NC];
     uint32_t vm[STEP][2][NG];   // V's (scale, zero) of keys g, g + 8
     float vd[STEP][2][NG];      // V's scales times S.down
+    uint32_t hidden[STEP];      // MASK: bit 2 NC nt + NC j + c where a column does not see a key of the lane
     float most = -INFINITY, top = 0.f;
 #pragma unroll
     for (int k = 0; k < STEP; ++k) {
         kv4_scores<D, ROWS>(blk + k * BLOCK, Q, s[k]);
+        hidden[k] = 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             bool seen = !MASK;
@@ -552,8 +554,12 @@ __device__ __forceinline__ void kv4_step(const uint8_t* blk, const Kv4Query<D, R
                     y = fmaf(s[k][nt][NC * j + c], Q.mul[nt][c], S.nm[nt][c]);
                     if (MASK) {
                         const int key = pos + 16 * k + g + 8 * j;
-                        if (key < lo[nt][c] || key >= hi[nt][c] || (gone >> k & 1)) y = -INFINITY;
-                        seen = seen || y != -INFINITY;
+                        if (key < lo[nt][c] || key >= hi[nt][c] || (gone >> k & 1)) {
+                            y = -INFINITY;
+                            hidden[k] |= 1u << (2 * NC * nt + NC * j + c);
+                        } else {
+                            seen = true;
+                        }
                     }
                 }
             kv4_pairs<NG>(blk + k * BLOCK + 17 * D + (g + 8 * j) * (NG * 4), vm[k][j]);
@@ -677,8 +683,9 @@ __device__ __forceinline__ void kv4_step(const uint8_t* blk, const Kv4Query<D, R
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         const float w = p[nt][NC * j + c];
-                        // a key that another column sees may hold a NaN that this one must not
-                        const bool none = MASK && w == 0.f;
+                        // a key that another column sees may hold a NaN that this one must not; under a weight that came
+                        // out as 0 it is a NaN here too
+                        const bool none = MASK && (hidden[k] >> (2 * NC * nt + NC * j + c) & 1);
                         ps[c] = none ? 0.f : w * sd;
                         S.z[nt][i][c] = none ? S.z[nt][i][c] : fmaf(w, ze, S.z[nt][i][c]);
                     }

@@ -57,3 +57,26 @@ def test_values_of_very_different_sizes(D, Hq, Hkv, B, n):
         o, lse = cz.attn_kv4(q.cuda(), pages, table, i32([n] * B), partial=True)
         check_few(q, pages, table, n, o, lse, (0, B - 1), partial=True)
     assert cz.get_device_status() == 0
+
+
+@pytest.mark.parametrize("D,T,Hq", [(64, 1, 1), (64, 2, 8), (128, 1, 4), (128, 2, 3), (256, 1, 2)])
+@pytest.mark.parametrize("at", [0, 5, 70, 150, 199])
+def test_a_value_that_is_not_a_number_under_no_weight(D, T, Hq, at):
+    """0 times NaN is NaN for every row that sees the key, wherever it stands; rows that do not see it are clean."""
+    n = 200
+    k, v = rows(1, 1, n, D, 1), rows(1, 1, n, D, 2)
+    k[0, 0, at] = -128.0                              # some 128 0.8 sqrt(D) below the others: its weight is 0
+    v[0, 0, at, D - 1] = float("nan")
+    q = rows(1, Hq, T, D, 3).abs()
+    pages, table = paged(1, 1, D, 16, n, 4)
+    cz.kv4_write(pages, table, i32([0]), k.cuda(), v.cuda())
+    o, lse = cz.attn_kv4(q.cuda(), pages, table, i32([n]))
+    assert torch.isfinite(lse).all()
+    for t in range(T):
+        sees = at <= n - T + t
+        assert torch.isnan(o[0, :, t, D - 64:]).all() == sees
+        assert torch.isfinite(o[0, :, t, :D - 64]).all()
+        if not sees:
+            assert torch.isfinite(o[0, :, t]).all()
+    o, lse = cz.attn_kv4(q.cuda(), pages, table, i32([n]), window=n - 100)
+    assert torch.isnan(o[..., D - 64:]).any() == (at > 100 - T)
