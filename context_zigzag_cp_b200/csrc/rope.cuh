@@ -10,8 +10,9 @@
 // The angle.  Only its fraction of a full turn matters, so it is taken in
 // 64-bit fixed point: F = frac(inv_freq / 2 pi) * 2^64, and position * F modulo
 // 2^64 is that fraction, exact for every int32 position (a far position in fp32
-// would lose it: 1e6 * 2^-24 rad).  Its top 32 bits, as a signed fraction of
-// half a turn, go to sincospif.
+// would lose it: 1e6 * 2^-24 rad).  What it has beyond the nearest quarter turn is taken
+// with 24 bits of its own, so that a small sine or cosine is right relative to itself (the
+// top 32 bits of the turn were not: 6e-4 of the sine of 2.5e-6 rad).
 //
 // Bound by HBM (4 bytes a value against 3 flops).  A thread keeps one octet of
 // pairs (16 values, two 16-byte vectors) of one token and walks the heads of
@@ -54,6 +55,22 @@ __device__ __forceinline__ unsigned long long rope_turns(double f)
     const double fr = p - floor(p);
     const unsigned long long hi = static_cast<unsigned long long>(fr * 18446744073709551616.0);
     return hi + static_cast<unsigned long long>(static_cast<long long>(e * 18446744073709551616.0));
+}
+
+// Sine and cosine of |x| <= pi / 4 by their Taylor series: what is left out is x^10 / 11! = 2.2e-9 and x^12 / 12! =
+// 1.2e-10 of them at most, below fp32's own 6e-8.
+__device__ __forceinline__ void rope_sincos(float x, float& s, float& c)
+{
+    const float z = x * x;
+    float p = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+    p = fmaf(z, p, 1.f / 120.f);
+    p = fmaf(z, p, -1.f / 6.f);
+    s = fmaf(x * z, p, x);
+    p = fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
+    p = fmaf(z, p, -1.f / 720.f);
+    p = fmaf(z, p, 1.f / 24.f);
+    p = fmaf(z, p, -0.5f);
+    c = fmaf(z, p, 1.f);
 }
 
 __device__ __forceinline__ void rope_unpack(const uint4& v, float (&x)[8])
@@ -124,10 +141,13 @@ __global__ void __launch_bounds__(256, HALF ? 2 : 4) rope_kernel(RopeParams P)
                 if (a < P.n_axes && pair >= P.sec_end[a - 1]) p = pos[a];
             const unsigned long long t =
                 static_cast<unsigned long long>(static_cast<long long>(p)) * rope_turns(P.inv_freq[pair]);
+            const unsigned quarter = static_cast<unsigned>((t + (1ull << 61)) >> 62);
+            const long long rest = static_cast<long long>(t - (static_cast<unsigned long long>(quarter) << 62));
             float s, c;
-            sincospif(static_cast<float>(static_cast<int>(t >> 32)) * 4.656612873077393e-10f, &s, &c);
-            cs[i] = c;
-            sn[i] = P.inverse ? -s : s;
+            rope_sincos(static_cast<float>(rest) * 3.4061215800865545e-19f, s, c);   // pi 2^-63
+            const float a = quarter & 1 ? c : s, b = quarter & 1 ? s : c;
+            cs[i] = (quarter + 1) & 2 ? -b : b;
+            sn[i] = (quarter & 2) != 0 != (P.inverse != 0) ? -a : a;
         }
     }
 
