@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcpattn.so")
@@ -135,15 +136,32 @@ def load() -> ctypes.CDLL:
 _calls = None
 
 
+class _PythonCalls:
+    """In place of the native part where there is none: takes nothing, so that Python marshals every call."""
+
+    @staticmethod
+    def rope(*args):
+        return None
+
+    kv4_write = kv4_read = attn_kv4 = rope
+
+
 def calls():
-    """The binding's native part (csrc/calls.cpp), handed the library's functions."""
+    """The binding's native part (csrc/calls.cpp), handed the library's functions.  Built for another torch, whose
+    classes may be laid out otherwise, it is not used."""
     global _calls
     if _calls is None:
         lib = load()
         try:
             from . import _calls as native
+            from .build import calls_mark
+            if native.__doc__ != calls_mark():
+                raise ImportError(f"_calls.so is {native.__doc__}, not {calls_mark()}")
         except ImportError as e:
-            raise ImportError("_calls.so not built; run `python -m context_zigzag_cp_b200.build`") from e
+            warnings.warn(f"{e}: the decoding calls go through Python, some 25 us slower; run "
+                          "`python -m context_zigzag_cp_b200.build`")
+            _calls = _PythonCalls
+            return _calls
         native.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
                       (lib.cp_rope, lib.cp_kv4_write, lib.cp_kv4_read, lib.cp_attn_kv4)))
         _calls = native

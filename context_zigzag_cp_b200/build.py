@@ -7,6 +7,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(_HERE)
@@ -50,6 +51,19 @@ def _run(cmd, target, verbose):
     os.replace(tmp, target)
 
 
+def calls_mark() -> str:
+    """What _calls.so says of the torch that it was built against: its classes are that torch's alone."""
+    import torch
+    return f"built for torch {torch.__version__}"
+
+
+def calls_up_to_date() -> bool:
+    if not _newer(CALLS, [CALLS_SRC, os.path.join(ROOT, "include", "cp_attn.h")]):
+        return False
+    with open(CALLS, "rb") as f:
+        return calls_mark().encode() + b"\0" in f.read()
+
+
 def _build_calls(verbose: bool) -> None:
     """_calls.so against the installed torch, whose allocator and streams it uses."""
     import torch
@@ -60,7 +74,7 @@ def _build_calls(verbose: bool) -> None:
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
     libs = os.path.join(root, "lib")
     _run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + ["-I" + i for i in inc] +
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DCALLS_MARK="{calls_mark()}"'] + ["-I" + i for i in inc] +
          [CALLS_SRC, "-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"],
          CALLS, verbose)
 
@@ -68,8 +82,11 @@ def _build_calls(verbose: bool) -> None:
 def build(force: bool = False, verbose: bool = False) -> str:
     if force or not up_to_date():
         _run([_nvcc()] + NVCC_FLAGS + ["-I", os.path.join(ROOT, "include"), SRC], LIB, verbose)
-    if force or not _newer(CALLS, [CALLS_SRC, os.path.join(ROOT, "include", "cp_attn.h")]):
-        _build_calls(verbose)
+    if force or not calls_up_to_date():
+        try:
+            _build_calls(verbose)
+        except (RuntimeError, OSError) as e:   # no g++, no headers of torch: the library itself does without
+            warnings.warn(f"_calls.so: {e}; the decoding calls go through Python, some 25 us slower")
     return LIB
 
 

@@ -376,7 +376,8 @@ PyMethodDef g_methods[] = {
     {nullptr, nullptr, 0, nullptr},
 };
 
-PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
+// The doc string names the torch that this was built for; the binding compares it.
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", CALLS_MARK, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
