@@ -1349,6 +1349,8 @@ extern "C" cp_status_t cp_kv4_read(const cp_kv4_cache_t* c, int32_t n_tokens, co
     cp_status_t st = check_kv4_rows(c, n_tokens, start, rows, n_rows, k, v);
     if (st != CP_OK) return st;
     if (c->batch == 0 || n_tokens == 0) return CP_OK;
+    const int64_t n_out = static_cast<int64_t>(c->batch) * c->num_kv_heads * n_rows * c->head_dim * 2;
+    if (overlap(k, n_out, v, n_out)) return CP_ERR_INVALID_ARG;
     Kv4RowsParams P = kv4_rows(c, n_tokens, start, counts, rows, n_rows);
     P.k_out = static_cast<__nv_bfloat16*>(k);
     P.v_out = static_cast<__nv_bfloat16*>(v);

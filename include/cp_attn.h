@@ -523,8 +523,8 @@ CP_API cp_status_t cp_kv4_write(const cp_kv4_cache_t* cache, int32_t n_tokens, c
 /*
  * cp_kv4_read -- the values that the cache holds for positions start[b] + t, t < counts[b],
  * as bf16 (zero + scale * code, one fp32 operation, rounded to bf16) in k, v [batch][Hkv][n_rows][D],
- * contiguous; rows as in cp_kv4_write, but distinct.  Rows that no token goes to
- * are left as they were.
+ * contiguous, which do not overlap; rows as in cp_kv4_write, but distinct.  Rows that no token
+ * goes to are left as they were.
  * Errors: as cp_kv4_write.
  */
 CP_API cp_status_t cp_kv4_read(const cp_kv4_cache_t* cache, int32_t n_tokens, const int32_t* start,

@@ -43,3 +43,15 @@ def test_in_place_where_an_extent_is_one(B, H, N):
     else:
         with pytest.raises(cz.CPError):
             call()
+
+
+def test_keys_and_values_read_into_one_tensor():
+    """Refused: rows of both would go to the same place."""
+    pages, table = filled([40], 2, 64, 32, 1)
+    out = torch.zeros(2, 2, 40, 64, dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(), dict(stream=torch.cuda.current_stream())):
+        with pytest.raises(cz.CPError):
+            cz.kv4_read(pages, table, i32([0]), 40, 64, k=out[:1], v=out[:1], **kw)
+        k, v = cz.kv4_read(pages, table, i32([0]), 40, 64, k=out[:1], v=out[1:], **kw)
+        assert torch.equal(k, cz.kv4_read(pages, table, i32([0]), 40, 64)[0])
+        assert torch.equal(v, cz.kv4_read(pages, table, i32([0]), 40, 64)[1])
