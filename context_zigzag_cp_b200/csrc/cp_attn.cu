@@ -1120,7 +1120,8 @@ cp_status_t check_kv4(const cp_kv4_cache_t* c)
     if (c->batch < 0 || c->num_kv_heads < 1 || c->num_pages < 1 || c->table_width < 0) return CP_ERR_INVALID_ARG;
     if (c->page_size < 16 || c->page_size % 16 != 0 || c->page_size > 65536) return CP_ERR_INVALID_ARG;
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return CP_ERR_UNSUPPORTED;
-    if (!c->pages || !aligned16(c->pages) || !c->block_table) return CP_ERR_INVALID_ARG;
+    if (!c->pages || !aligned16(c->pages)) return CP_ERR_INVALID_ARG;
+    if (!c->block_table && c->table_width > 0) return CP_ERR_INVALID_ARG;   // a table without columns has no address
     // positions and flat (sequence, head) indices are int32
     if (static_cast<int64_t>(c->table_width) * c->page_size > (1 << 30)) return CP_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(c->batch) * c->num_kv_heads > (1 << 24)) return CP_ERR_UNSUPPORTED;

@@ -481,7 +481,7 @@ CP_API cp_status_t cp_rope(const cp_rope_t* rope, const cp_problem_t* problem, c
  *   D 128    64 r + 16 t + 4 w                              128 g + 16 (p ^ 4 (g % 2)) + 8 b + 4 n
  *   D 256    128 r + 64 (w / 4 ^ r % 2) + 16 t + 4 (w % 4)  256 g + 32 p + 16 (b ^ g % 2) + 4 n
  * Token i of sequence b is in page block_table[b][i / page_size], row i % page_size
- * (DEVICE int32 [batch][table_width]).  Several sequences may share pages that are
+ * (DEVICE int32 [batch][table_width]; may be NULL where table_width is 0).  Several sequences may share pages that are
  * only read.  A page outside [0, num_pages), or a position beyond the table,
  * records CP_ERR_INVALID_ARG in the device status word and is left out: nothing
  * outside the pool is read or written.

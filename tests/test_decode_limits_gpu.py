@@ -55,3 +55,20 @@ def test_keys_and_values_read_into_one_tensor():
         k, v = cz.kv4_read(pages, table, i32([0]), 40, 64, k=out[:1], v=out[1:], **kw)
         assert torch.equal(k, cz.kv4_read(pages, table, i32([0]), 40, 64)[0])
         assert torch.equal(v, cz.kv4_read(pages, table, i32([0]), 40, 64)[1])
+
+
+@pytest.mark.parametrize("B,T", [(1, 1), (3, 4), (200, 1)])
+def test_a_table_without_pages(B, T):
+    """Sequences that hold nothing yet: O = 0, LSE = -inf; a token has no place there."""
+    pages, _ = filled([16], 2, 64, 16, 1)
+    before = pages.clone()
+    table = torch.zeros(B, 0, dtype=torch.int32, device="cuda")
+    for kw in (dict(), dict(causal=False), dict(window=3)):
+        o, lse = cz.attn_kv4(rows(B, 4, T, 64, 2).cuda(), pages, table, i32([0] * B), **kw)
+        assert (o == 0).all() and (lse == float("-inf")).all()
+    assert cz.get_device_status() == 0
+    k = rows(B, 2, T, 64, 3).cuda()
+    cz.kv4_write(pages, table, i32([0] * B), k, k)
+    assert cz.get_device_status() == 1 and torch.equal(pages, before)
+    got = cz.kv4_read(pages, table, i32([0] * B), T, 64, k=k.clone(), v=k.clone())
+    assert cz.get_device_status() == 1 and torch.equal(got[0], k) and torch.equal(got[1], k)
