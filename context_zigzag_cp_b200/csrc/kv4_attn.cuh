@@ -67,9 +67,11 @@ namespace cpattn {
 
 constexpr int KV4_TILE = 64;         // keys of a scheduling tile (four 16-key blocks)
 constexpr uint32_t KV4_NONE = 0xffffffffu;
-// Tiles that one CTA takes alone: a stage or two a warp, less than a join costs.  (301 keys 5.3 us, split 8.6; 16
-// sequences of up to 400 keys 5.8, split 10.2.)
-constexpr int KV4_WHOLE = 8;
+// Tiles that one CTA takes alone: two stages a warp, no more than a join and its launch cost.  Whole / split, us, one
+// sequence and 18 of 32 / 8 heads of 128 dims, 4 rows a unit: up to 447 keys 5.8 / 9.0 and 6.1 / 11.0, 1023 keys 7.8 / 9.0
+// and 8.2 / 13.6; above it one sequence is behind, 1279 keys 9.4 / 9.1 and 9.7 / 13.8, 2047 keys 11.4 / 9.0 and 11.7 /
+// 15.3.  At 1023 keys of 256 dims 11.8 / 11.5 for one and 12.3 / 14.5 for 30, of 64 dims 6.2 / 7.5 for one.
+constexpr int KV4_WHOLE = 16;
 
 // ROWS: query rows a unit, 4 (PAIR), 8, or 16 (two n-tiles; not at D 256, where O alone would take
 // 128 registers).  BPS: blocks of a stage, in which they are copied and

@@ -72,3 +72,16 @@ def test_a_table_without_pages(B, T):
     assert cz.get_device_status() == 1 and torch.equal(pages, before)
     got = cz.kv4_read(pages, table, i32([0] * B), T, 64, k=k.clone(), v=k.clone())
     assert cz.get_device_status() == 1 and torch.equal(got[0], k) and torch.equal(got[1], k)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,D,most,window", [(1, 4, 1, 128, 1023, 0), (1, 4, 1, 128, 1024, 0), (18, 16, 8, 64, 1023, 0),
+                                                    (19, 16, 8, 64, 1023, 0), (3, 8, 2, 256, 1008, 0),
+                                                    (2, 16, 1, 128, 3000, 1020), (2, 16, 1, 128, 3000, 1023)])
+def test_tables_and_windows_around_what_one_cta_takes_alone(B, Hq, Hkv, D, most, window):
+    lens = [most - 37 * b for b in range(B)]
+    lens[-1] = max(lens[-1], 1)
+    pages, table = filled(lens, Hkv, D, 16, 5)
+    q = rows(B, Hq, 1, D, 6)
+    o, lse = cz.attn_kv4(q.cuda(), pages, table, i32(lens), window=window)
+    check_attn(q, pages, table, lens, o, lse, window=window)
+    assert cz.get_device_status() == 0
