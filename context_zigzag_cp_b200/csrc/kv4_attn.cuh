@@ -46,9 +46,12 @@
 //     119 us for 64 ragged sequences, 1 to 1.6 of 44 to 52 us at head_dim 256.)
 //   - One CTA of eight warps an SM and 64 keys computed together: two warps a scheduler fill
 //     the integer pipe as well as more do, and what a stage costs is paid half as often (64
-//     ragged sequences of up to 16k keys, 32 / 8 heads of 128 dims: 115 us = 5.9 TB/s; 16 warps and
-//     32 keys 125 us, 11 and 12 warps 118 to 123).  128k keys of one sequence: 34.5 us, of which
-//     25 stream at 6.0 TB/s and the rest is start, join and merge.
+//     ragged sequences of up to 16k keys, 32 / 8 heads of 128 dims: 115 us; 16 warps and 32
+//     keys 125 us, 11 and 12 warps 118 to 123).  That is 5.9 TB/s with an L2 that nothing else
+//     writes; among other kernels it is 133 us, 5.1 TB/s.  128k keys of one sequence: 34.5 us, of
+//     which 25 stream at 6.0 TB/s and the rest is start, join and merge.
+//   - Rows beyond a block of 16 (8 at D 256) pass over the keys again: 8 tokens of 16 heads a KV
+//     head, 16 sequences of up to 8k keys, take 69 us for 3.8 us of bytes (D 256: 150 for 7.6).
 //
 // Work split.  The warps of all CTAs share all key tiles of all (sequence, KV head, row
 // block) units evenly: with the units laid end to end, warp v of n takes the tiles

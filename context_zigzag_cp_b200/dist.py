@@ -31,7 +31,8 @@ Decoding after a context (decode): every rank keeps the keys and values of its o
 rows in a 4-bit cache (cp_kv4_write on its shard; a context's order inside the
 cache does not matter to later tokens, which see all of it), the tokens that
 follow go to one rank's cache, and their attention (cp_attn_kv4 on every rank's
-part) is joined by one all-gather of the partials and the LSE-merge kernel.
+part) is joined by one all-gather of the partials and the LSE-merge kernel.  Problems
+with a window, documents or no causal mask are refused there.
 
 The library moves no data between GPUs; this module runs the collectives with
 torch.distributed (NCCL on GPUs).  The kernel calls go through a `kernels`

@@ -500,7 +500,8 @@ typedef struct {
 /*
  * cp_kv4_write -- quantise new rows of K and V into the cache.  Token t of sequence b,
  * t < counts[b], goes to position start[b] + t.  Per group: zero = min, scale =
- * bf16((max - min) / 15), code = (x - zero) / scale to nearest, ties to even (a
+ * bf16((max - min) / 15), code = (x - zero) / scale to nearest, ties to even, x - zero in fp32
+ * (which rounds it where the two are 2^16 apart or more; a
  * scale below 2^-126 becomes 0, all codes 0).  A group that holds a NaN or an
  * infinity, or whose max - min overflows, gets a NaN scale and reads back as NaN.
  *   n_tokens    tokens of a sequence at most (T); start, counts DEVICE int32
