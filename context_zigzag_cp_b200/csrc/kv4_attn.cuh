@@ -638,7 +638,8 @@ __device__ __forceinline__ void kv4_step(const uint8_t* blk, const Kv4Query<D, R
             const int least_e = __reduce_min_sync(0xffffffffu, v > 0.f ? __float_as_uint(v) : 0x7f800000u) >> 23;
             const int w_e = __reduce_max_sync(0xffffffffu, __float_as_uint(w)) >> 23;
             const int old = kv4_exp(S.down[i]);
-            int e = min(most_e, max(max(w_e + 10, least_e + 8), old));   // most_e where it is no more than old
+            // most_e where that is no more than old; a scale times S.down stays finite, 2^(most_e + 7 - e) at most
+            int e = min(most_e, max(max(max(w_e + 10, least_e + 8), old), most_e - 120));
             e = e >= old ? e : e > 0 && e + 7 < old ? max(e, max(old - 60, 27)) : old;
             const float fe = pow2i(max(old - e, -126));
             S.down[i] = pow2i(133 - e);

@@ -80,3 +80,18 @@ def test_a_value_that_is_not_a_number_under_no_weight(D, T, Hq, at):
             assert torch.isfinite(o[0, :, t]).all()
     o, lse = cz.attn_kv4(q.cuda(), pages, table, i32([n]), window=n - 100)
     assert torch.isnan(o[..., D - 64:]).any() == (at > 100 - T)
+
+
+@pytest.mark.parametrize("D,Hq,B,n", [(64, 4, 2, 300), (128, 3, 48, 1024), (256, 8, 2, 700), (128, 16, 2, 3000)])
+def test_values_at_the_ends_of_their_type(D, Hq, B, n):
+    """Small values beside keys with the largest ones that bf16 has, which no row gives weight."""
+    def change(k, v):
+        v *= 2.0 ** -12
+        for at in (3, n // 2, n - 2):
+            k[:, :, at] = -64.0
+            v[:, :, at] = v[:, :, at].sign() * 2.0 ** 126
+    q = rows(B, Hq, 1, D, 5).abs()
+    pages, table = spread_cache(B, 1, D, n, 20, change)
+    o, lse = cz.attn_kv4(q.cuda(), pages, table, i32([n] * B), partial=True)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    check_few(q, pages, table, n, o, lse, (0, B - 1), partial=True)
